@@ -491,7 +491,12 @@ log_probs_kernel(const LogProbsArgs a, int64_t slice) {
                 exchange_store(exchange_addr(&s_all[rank * kTop + threadIdx.x], 0), s_best[threadIdx.x], arrived);
         }
         if (kStages <= 3) pdl_launch_dependents();
-        if (rank != 0 || !exchange_wait(&s_arrived, a.wait_limit)) return;
+        if (rank != 0) return;
+        // The list and its count are empty before any warp adds to them: the
+        // bytes that end the wait may come while a warp is still before its
+        // reset.  (The barrier's time passes beside the exchange's.)
+        __syncthreads();
+        if (!exchange_wait(&s_arrived, a.wait_limit)) return;
         if (warp == 0) {
             const float4 part = s_parts[lane % kMaxCluster];
             st = join_warp<true, kMaxCluster>(lane % kMaxCluster < ranks ? State{part.x, part.y, part.z} : none);
