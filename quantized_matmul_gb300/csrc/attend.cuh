@@ -613,10 +613,12 @@ attend_kernel(const AttendArgs a) {
                             largest = __hmax2(largest, __habs2(reinterpret_cast<const __half2 &>(d[s][j][c])));
                 }
             if constexpr (NB % 2 == 0) {  // the words hold scales alone: a lane looks at a part of them
+                constexpr int kWords = T::kTokens * T::kScaleWords;  // 48 where d is 192; row numbers lie behind
                 const __half2 *words = reinterpret_cast<const __half2 *>(stage + 2 * T::kPlane + T::kScales);
 #pragma unroll
-                for (int c = 0; c < T::kTokens * T::kScaleWords; c += 32)
-                    largest = __hmax2(largest, __habs2(words[c + lane]));
+                for (int c = 0; c < kWords; c += 32)
+                    if (kWords % 32 == 0 || c + lane < kWords)
+                        largest = __hmax2(largest, __habs2(words[c + lane]));
             }
         }
         bool move = Q8 && !__hble2(largest, most_d);

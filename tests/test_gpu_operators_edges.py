@@ -4,7 +4,8 @@ tolerances they share."""
 import numpy as np
 import pytest
 
-from test_gpu_operators import check_log_probs, rng_of, up
+import test_gpu_operators as base
+from test_gpu_operators import check_attention, check_log_probs, make_cache, rng_of, run_attention, up
 
 pytestmark = pytest.mark.gpu
 
@@ -12,6 +13,57 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture
 def torch():
     return pytest.importorskip("torch")
+
+
+# ---------------------------------------------------------------------------
+# attention
+
+@pytest.mark.parametrize("fmt", ["f16", "q8_0"])
+@pytest.mark.parametrize("scale", [0.02, 1e-4])
+@pytest.mark.parametrize("first", [31488, 65536 + 31488])
+@pytest.mark.parametrize("d", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_attention_does_not_depend_on_where_the_pages_lie(qmm, torch, fmt, d, first, scale):
+    """The same tokens in the cache's first pages and in pages from row `first` on, whose number's bits
+    would be a large f16: the same bits out.  For one sequence and a ragged batch."""
+    g = rng_of(31, d)
+    kv_heads, ps, used = 2, 16, 38
+    planes = make_cache(g, fmt, used, kv_heads, ps, d)
+    if fmt == "q8_0":
+        planes[3] = (scale * (0.5 + g.random(planes[3].shape))).astype(np.float16)
+    at = first // (kv_heads * ps)
+    low, high = [up(p) for p in planes], []
+    for p in low:
+        high.append(torch.zeros((at + used,) + p.shape[1:], dtype=p.dtype, device="cuda"))
+        high[-1][at:] = p
+    for lens in ([300], [40, 300]):
+        table = g.permutation(used).astype(np.int32)[: 19 * len(lens)].reshape(len(lens), 19)
+        q = up(g.standard_normal((len(lens), 6 * d), np.float32))
+        n = up(np.array(lens, np.int32))
+        want = run_attention(qmm, fmt, q, low, up(table), n)
+        got = run_attention(qmm, fmt, q, high, up(table + at), n)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("d", [160, 192, 224])
+def test_attention_q8_0_in_pages_of_large_row_numbers(qmm, d):
+    g = rng_of(32, d)
+    check_attention(qmm, 32, "q8_0", 4, 2, d, 16, [300, 150],
+                    table=(984 + g.permutation(38)).astype(np.int32).reshape(2, 19),
+                    planes=make_cache(g, "q8_0", 984 + 38, 2, 16, d))
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8_0"])
+@pytest.mark.parametrize("heads", [1, 5, 8, 11])
+def test_attention_with_heads_of_192_within_a_cluster(qmm, fmt, heads):
+    for n in (129, 577, 897, 1024):
+        check_attention(qmm, n, fmt, heads, 1, 192, 16, [n])
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8_0"])
+@pytest.mark.parametrize("garbage", [np.nan, -np.inf, 65504.0])
+@pytest.mark.parametrize("d", [32, 160, 192, 224, 256])
+def test_attention_of_other_head_sizes_ignores_what_it_does_not_attend_to(qmm, torch, fmt, garbage, d):
+    base.test_attention_ignores_what_it_does_not_attend_to(qmm, torch, fmt, garbage, d)
 
 
 # ---------------------------------------------------------------------------
