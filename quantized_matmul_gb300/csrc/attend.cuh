@@ -25,15 +25,15 @@
 // hi + lo, hi = f16(f), lo = f16(f - hi), which keep 22 bits.  The cache is
 // the MMA's A operand (16 tokens for the scores, 16 elements of the values
 // for the output); the 8 columns of B are 4 heads' hi and lo in turn, so a
-// lane's two neighbouring accumulators add up to a head's product.  Powers of
+// lane's two neighbouring accumulators add up to a head's product.  The MMA
+// sums one tile's tokens, f32 additions the tiles.  Powers of
 // two keep both in f16's range: a head's q is scaled to its largest element,
 // the weights by 2^11 and what the largest value scale needs (Q8_0); the
 // outputs are held times that power.
 //
 // The softmax's base need not be the running maximum: weights up to 2^4 fit,
 // so the base (and with it the outputs so far) moves only when a score passes
-// it by more than 4 binary orders, which costs a warp one vote a tile.  The
-// output stays in the MMA's accumulators meanwhile.
+// it by more than 4 binary orders, which costs a warp one vote a tile.
 //
 // Q8_0: a score takes a block's product times the key's scale, block after
 // block.  A value's scale d multiplies the weight's halves: hi = f16(w_hi d),
@@ -352,7 +352,7 @@ struct Tile {
     // cache) or times `lift` and their scales in d (Q8_0)
     static __device__ __forceinline__ void weigh(const char *stage, int lane, const float (&p)[kSub][2][NT],
                                                  float lift, const uint32_t (&d)[Q8 ? kSub : 1][4][kPairs],
-                                                 float (&o)[kRowsOut][NT][4]) {
+                                                 float (&o)[kRowsOut][NT][2]) {
         const int g = lane >> 2, t = lane & 3;
         // From the scores' layout (tokens g, g + 8 of head t) to the weights'
         // (tokens 2t, 2t + 1, 2t + 8, 2t + 9 of head g / 2, hi where g is even):
@@ -385,16 +385,22 @@ struct Tile {
             const uint32_t from = shared_addr(stage) + kPlane + ((lane >> 4) * 8 + (lane & 7)) * kStride +
                                   ((lane >> 3) & 1) * 16;
 #pragma unroll
-            for (int c = 0; c < kRowsOut; ++c)
+            for (int c = 0; c < kRowsOut; ++c) {
+                float x[NT][4];
 #pragma unroll
                 for (int s = 0; s < kSub; ++s) {
                     const uint4 v = load_matrices<true>(from + 16 * s * kStride + 32 * c);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_16816(o[c][n], v, w[s][n]);
+                    for (int n = 0; n < NT; ++n)
+                        if (s == 0) mma_16816_first(x[n], v, w[s][n]);
+                        else mma_16816(x[n], v, w[s][n]);
                 }
+                add(x, o[c]);
+            }
         } else {
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b) {
+                float x0[NT][4], x1[NT][4];
 #pragma unroll
                 for (int s = 0; s < kSub; ++s) {
                     const uint32_t d0 = __byte_perm(d[s][0][b / 2], d[s][1][b / 2], b & 1 ? 0x7632 : 0x5410);
@@ -420,11 +426,29 @@ struct Tile {
                     for (int n = 0; n < NT; ++n) {
                         const uint2 wd = {scale_half(w[s][n].x, w_lo[s][n].x, d0),
                                           scale_half(w[s][n].y, w_lo[s][n].y, d1)};
-                        mma_16816(o[2 * b][n], v0, wd);
-                        mma_16816(o[2 * b + 1][n], v1, wd);
+                        if (s == 0) {
+                            mma_16816_first(x0[n], v0, wd);
+                            mma_16816_first(x1[n], v1, wd);
+                        } else {
+                            mma_16816(x0[n], v0, wd);
+                            mma_16816(x1[n], v1, wd);
+                        }
                     }
                 }
+                add(x0, o[2 * b]);
+                add(x1, o[2 * b + 1]);
+            }
         }
+    }
+
+    // A tile's products, the weights' halves joined, to the outputs.  The MMA
+    // truncates what it adds to its accumulators, and always towards zero: over
+    // a long sequence's tiles that would add up (32768 tokens of one split: 9e-6
+    // of the output with f16, 4e-5 with Q8_0; a sum rounded to nearest 2e-7), so
+    // only the products of one tile are summed there.
+    static __device__ __forceinline__ void add(const float (&x)[NT][4], float (&o)[NT][2]) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][0] += x[n][0] + x[n][1], o[n][1] += x[n][2] + x[n][3];
     }
 
     // the element that row g (i = 0) or g + 8 (i = 1) of output tile c stands for
@@ -567,9 +591,9 @@ attend_kernel(const AttendArgs a) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) scale[n] = s_scale[4 * n + t];
 
-    // o: tiles of 16 elements times columns 2t (hi) and 2t + 1 (lo) of head t,
-    // times `lift`; l: the sum of this lane's weights, both relative to 2^base
-    float o[T::kRowsOut][NT][4] = {}, base[NT], l[NT] = {};
+    // o: elements g and g + 8 of each tile of 16, of head t, times `lift`; l: the
+    // sum of this lane's weights, both relative to 2^base
+    float o[T::kRowsOut][NT][2] = {}, base[NT], l[NT] = {};
 #pragma unroll
     for (int n = 0; n < NT; ++n) base[n] = -INFINITY;
     float lift = T::kLift;
@@ -662,7 +686,7 @@ attend_kernel(const AttendArgs a) {
 #pragma unroll
                 for (int c = 0; c < T::kRowsOut; ++c)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[c][n][j] *= alpha * ratio;
+                    for (int j = 0; j < 2; ++j) o[c][n][j] *= alpha * ratio;
 #pragma unroll
                 for (int s = 0; s < T::kSub; ++s)
 #pragma unroll
@@ -709,8 +733,7 @@ attend_kernel(const AttendArgs a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                s_o[(warp * H + 4 * n + t) * D + T::element(c, i, g)] =
-                    (o[c][n][2 * i] + o[c][n][2 * i + 1]) * lift_inv;
+                s_o[(warp * H + 4 * n + t) * D + T::element(c, i, g)] = o[c][n][i] * lift_inv;
     __syncthreads();
     const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.ldo * 4) & 15) == 0;
     auto finish = [&](int h, int e, float top, float sum, const float (&acc)[4]) {

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 
 import test_gpu_operators as base
-from test_gpu_operators import check_attention, check_log_probs, make_cache, rng_of, run_attention, up
+from test_gpu_operators import EPS32, check_attention, check_log_probs, make_cache, rng_of, run_attention, up
 
 pytestmark = pytest.mark.gpu
 
@@ -42,6 +42,40 @@ def test_attention_does_not_depend_on_where_the_pages_lie(qmm, torch, fmt, d, fi
         want = run_attention(qmm, fmt, q, low, up(table), n)
         got = run_attention(qmm, fmt, q, high, up(table + at), n)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("fmt", ["f16", "q8_0"])
+@pytest.mark.parametrize("d,kv_heads,n", [(32, 640, 32768), (128, 640, 8192), (256, 320, 8200)])
+def test_attention_of_long_sequences_without_splits(qmm, torch, fmt, d, kv_heads, n):
+    """A zero query and values above zero: the output is their mean, whose sum runs through n / 64 (n /
+    128 for d <= 64) tiles a warp.  Additions rounded to nearest are off by 2^-24 / sqrt(3) of a partial
+    sum each and independent, 2^-24 sqrt(tiles) / 3 in all; six times that, and four roundings (halves,
+    joins, the quotient), bound every element.  Their mean over all elements is a bias: the sums of one
+    tile (of at most 2^-23 for the order of 16 products and of its two halves) and the roundings after."""
+    page = 64
+    pages = -(-n // page)
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    shape = (pages, kv_heads, page, d)
+    if fmt == "f16":
+        v = torch.rand(shape, generator=gen, device="cuda", dtype=torch.float16)
+        planes, values = [v, v], v
+    else:
+        codes = torch.randint(0, 128, shape, generator=gen, device="cuda", dtype=torch.int8)
+        scales = torch.full(shape[:3] + (d // 32,), 0.0123, device="cuda", dtype=torch.float16)
+        planes, values = [codes, scales, codes, scales], codes
+    table = torch.arange(pages, device="cuda", dtype=torch.int32)[None]
+    lens = torch.tensor([n], device="cuda", dtype=torch.int32)
+    q = torch.zeros(1, kv_heads * d, device="cuda")
+    out, lse = run_attention(qmm, fmt, q, planes, table, lens)
+    total = torch.zeros(kv_heads, d, dtype=torch.float64, device="cuda")
+    for p in range(pages):
+        total += values[p, :, : min(page, n - p * page)].double().sum(1)
+    want = total / n * (float(np.float16(0.0123)) if fmt == "q8_0" else 1.0)
+    off = (out.view(kv_heads, d).double() - want) / want
+    tiles = n / (128 if d <= 64 else 64)
+    assert float(off.abs().max()) <= (6 * tiles ** 0.5 / 3 + 4) * EPS32
+    assert abs(float(off.mean())) <= 8 * EPS32
+    assert float((lse.double() - np.log(n)).abs().max()) <= (6 * tiles ** 0.5 / 3 + 16) * EPS32
 
 
 @pytest.mark.parametrize("d", [160, 192, 224])
