@@ -26,10 +26,8 @@
 // the MMA's A operand (16 tokens for the scores, 16 elements of the values
 // for the output); the 8 columns of B are 4 heads' hi and lo in turn, so a
 // lane's two neighbouring accumulators add up to a head's product.  The MMA
-// sums one tile's tokens, f32 additions the tiles.  Powers of
-// two keep both in f16's range: a head's q is scaled to its largest element,
-// the weights by 2^11 and what the largest value scale needs (Q8_0); the
-// outputs are held times that power.
+// sums one tile's tokens, f32 additions the tiles.  Powers of two keep both in
+// f16's range: a head's q is scaled to its largest element, the weights by 2^11.
 //
 // The softmax's base need not be the running maximum: weights up to 2^4 fit,
 // so the base (and with it the outputs so far) moves only when a score passes
@@ -38,6 +36,10 @@
 // Q8_0: a score takes a block's product times the key's scale, block after
 // block.  A value's scale d multiplies the weight's halves: hi = f16(w_hi d),
 // lo = f16(w_lo d + (w_hi d - hi)), the bracket exact by a fused multiply-add.
+// That takes scales of 2^-14 to 1 (or, times 2^10, up to 2^-10); tiles with
+// others form the product in f32 and give each block and head a power of two of
+// its own (64 ragged sequences with scales of 0.02 and 60 in a token: 72 us
+// against 63).
 #pragma once
 
 #include <type_traits>
@@ -348,10 +350,32 @@ struct Tile {
         }
     }
 
-    // o += weight times value over the tile, the weights times `lift` (f16
-    // cache) or times `lift` and their scales in d (Q8_0)
+    // Q8_0: block b's codes of 16 tokens as the MMA's A operands, elements 4 (lane / 4) + {0, 1}
+    // (v0) and + {2, 3} (v1)
+    static __device__ __forceinline__ void values(const char *stage, int lane, int s, int b, uint4 &v0, uint4 &v1) {
+        const int g = lane >> 2, t = lane & 3;
+        uint32_t lo[2], hi[2];  // bytes of a token pair, interleaved
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            uint32_t x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                x[j] = *reinterpret_cast<const uint32_t *>(
+                           stage + kPlane + offset(weight_token(s, 2 * i + j, t), 2 * b + (g >> 2)) + 4 * (g & 3)) ^
+                       0x80808080u;
+            lo[i] = __byte_perm(x[0], x[1], 0x5140);
+            hi[i] = __byte_perm(x[0], x[1], 0x7362);
+        }
+        v0 = {bytes_to_half2(lo[0], 0x4140), bytes_to_half2(lo[0], 0x4342), bytes_to_half2(lo[1], 0x4140),
+              bytes_to_half2(lo[1], 0x4342)};
+        v1 = {bytes_to_half2(hi[0], 0x4140), bytes_to_half2(hi[0], 0x4342), bytes_to_half2(hi[1], 0x4140),
+              bytes_to_half2(hi[1], 0x4342)};
+    }
+
+    // o += weight times value over the tile.  Q8_0: d holds the value scales
+    // times 2^up, none of them above 1.
     static __device__ __forceinline__ void weigh(const char *stage, int lane, const float (&p)[kSub][2][NT],
-                                                 float lift, const uint32_t (&d)[Q8 ? kSub : 1][4][kPairs],
+                                                 const uint32_t (&d)[Q8 ? kSub : 1][4][kPairs], int up,
                                                  float (&o)[kRowsOut][NT][2]) {
         const int g = lane >> 2, t = lane & 3;
         // From the scores' layout (tokens g, g + 8 of head t) to the weights'
@@ -365,7 +389,7 @@ struct Tile {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 uint32_t hi, lo;
-                split_pair(p[s][0][n] * lift, p[s][1][n] * lift, hi, lo);
+                split_pair(p[s][0][n] * kLift, p[s][1][n] * kLift, hi, lo);
                 uint32_t both[2][2];  // [token g or g + 8][source lane]
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -381,6 +405,7 @@ struct Tile {
                     w_lo[s][n] = {__byte_perm(both[0][0], both[0][1], pick), __byte_perm(both[1][0], both[1][1], pick)};
                 }
             }
+        const float down = 1.0f / kLift * (Q8 ? exp2i(-up) : 1.0f);
         if constexpr (!Q8) {
             const uint32_t from = shared_addr(stage) + kPlane + ((lane >> 4) * 8 + (lane & 7)) * kStride +
                                   ((lane >> 3) & 1) * 16;
@@ -395,7 +420,7 @@ struct Tile {
                         if (s == 0) mma_16816_first(x[n], v, w[s][n]);
                         else mma_16816(x[n], v, w[s][n]);
                 }
-                add(x, o[c]);
+                add(x, down, o[c]);
             }
         } else {
 #pragma unroll
@@ -405,23 +430,8 @@ struct Tile {
                 for (int s = 0; s < kSub; ++s) {
                     const uint32_t d0 = __byte_perm(d[s][0][b / 2], d[s][1][b / 2], b & 1 ? 0x7632 : 0x5410);
                     const uint32_t d1 = __byte_perm(d[s][2][b / 2], d[s][3][b / 2], b & 1 ? 0x7632 : 0x5410);
-                    uint32_t lo[2], hi[2];  // bytes of a token pair, interleaved
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t x[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            x[j] = *reinterpret_cast<const uint32_t *>(
-                                       stage + kPlane +
-                                       offset(weight_token(s, 2 * i + j, t), 2 * b + (g >> 2)) + 4 * (g & 3)) ^
-                                   0x80808080u;
-                        lo[i] = __byte_perm(x[0], x[1], 0x5140);
-                        hi[i] = __byte_perm(x[0], x[1], 0x7362);
-                    }
-                    const uint4 v0 = {bytes_to_half2(lo[0], 0x4140), bytes_to_half2(lo[0], 0x4342),
-                                      bytes_to_half2(lo[1], 0x4140), bytes_to_half2(lo[1], 0x4342)};
-                    const uint4 v1 = {bytes_to_half2(hi[0], 0x4140), bytes_to_half2(hi[0], 0x4342),
-                                      bytes_to_half2(hi[1], 0x4140), bytes_to_half2(hi[1], 0x4342)};
+                    uint4 v0, v1;
+                    values(stage, lane, s, b, v0, v1);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint2 wd = {scale_half(w[s][n].x, w_lo[s][n].x, d0),
@@ -435,20 +445,87 @@ struct Tile {
                         }
                     }
                 }
-                add(x0, o[2 * b]);
-                add(x1, o[2 * b + 1]);
+                add(x0, down, o[2 * b]);
+                add(x1, down, o[2 * b + 1]);
             }
         }
     }
 
-    // A tile's products, the weights' halves joined, to the outputs.  The MMA
+    // The same for value scales d of any size: a weight's product with its
+    // scale is taken in f32 and then halved, each block and head of a tile
+    // under a power of two of its own, which takes the largest product to
+    // [2^14, 2^15).
+    static __device__ __forceinline__ void weigh_any(const char *stage, int lane, const float (&p)[kSub][2][NT],
+                                                     const uint32_t (&d)[Q8 ? kSub : 1][4][kPairs],
+                                                     float (&o)[kRowsOut][NT][2]) {
+        const int g = lane >> 2, t = lane & 3, source = 8 * t + (g >> 1);
+        float w[kSub][NT][4];  // the weights' layout, as in weigh
+#pragma unroll
+        for (int s = 0; s < kSub; ++s)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[s][n][j] = __shfl_sync(0xffffffffu, p[s][j >> 1][n], source + 4 * (j & 1));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float x0[NT][4], x1[NT][4], up[NT], down[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float most = 0.0f;
+#pragma unroll
+                for (int s = 0; s < kSub; ++s)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        most = fmaxf(most, fabsf(w[s][n][j] * half_of(d[s][j][b / 2], b)));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                const int e = max(__float_as_int(most) >> 23, 15);  // most is below 2^(e - 126), 2^20
+                up[n] = exp2i(141 - e);
+                down[n] = __shfl_sync(0xffffffffu, exp2i(e - 141), 8 * t);  // the products' head is t, not g / 2
+            }
+#pragma unroll
+            for (int s = 0; s < kSub; ++s) {
+                uint4 v0, v1;
+                values(stage, lane, s, b, v0, v1);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[j] = w[s][n][j] * half_of(d[s][j][b / 2], b) * up[n];
+                    uint2 hi, lo;
+                    split_pair(x[0], x[1], hi.x, lo.x);
+                    split_pair(x[2], x[3], hi.y, lo.y);
+                    const uint2 wd = g & 1 ? lo : hi;
+                    if (s == 0) {
+                        mma_16816_first(x0[n], v0, wd);
+                        mma_16816_first(x1[n], v1, wd);
+                    } else {
+                        mma_16816(x0[n], v0, wd);
+                        mma_16816(x1[n], v1, wd);
+                    }
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    o[2 * b][n][i] = fmaf(x0[n][2 * i] + x0[n][2 * i + 1], down[n], o[2 * b][n][i]);
+                    o[2 * b + 1][n][i] = fmaf(x1[n][2 * i] + x1[n][2 * i + 1], down[n], o[2 * b + 1][n][i]);
+                }
+        }
+    }
+
+    // A tile's products, the weights' halves joined, times `down` to the outputs.  The MMA
     // truncates what it adds to its accumulators, and always towards zero: over
     // a long sequence's tiles that would add up (32768 tokens of one split: 9e-6
     // of the output with f16, 4e-5 with Q8_0; a sum rounded to nearest 2e-7), so
     // only the products of one tile are summed there.
-    static __device__ __forceinline__ void add(const float (&x)[NT][4], float (&o)[NT][2]) {
+    static __device__ __forceinline__ void add(const float (&x)[NT][4], float down, float (&o)[NT][2]) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) o[n][0] += x[n][0] + x[n][1], o[n][1] += x[n][2] + x[n][3];
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) o[n][i] = fmaf(x[n][2 * i] + x[n][2 * i + 1], down, o[n][i]);
     }
 
     // the element that row g (i = 0) or g + 8 (i = 1) of output tile c stands for
@@ -591,14 +668,16 @@ attend_kernel(const AttendArgs a) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) scale[n] = s_scale[4 * n + t];
 
-    // o: elements g and g + 8 of each tile of 16, of head t, times `lift`; l: the
-    // sum of this lane's weights, both relative to 2^base
+    // o: elements g and g + 8 of each tile of 16, of head t; l: the sum of this
+    // lane's weights, both relative to 2^base
     float o[T::kRowsOut][NT][2] = {}, base[NT], l[NT] = {};
 #pragma unroll
     for (int n = 0; n < NT; ++n) base[n] = -INFINITY;
-    float lift = T::kLift;
-    int lift_d = 0;                    // Q8_0: the value scales are taken times 2^lift_d
-    __half2 most_d = __half2half2(__float2half_rn(-1.0f));  // and the largest one that fits
+    // Q8_0: the value scales are taken times 2^up, 0 or 10, which fits tiles
+    // whose scales other than 0 lie in [least_d, most_d]; -1: each block has a
+    // power of its own (weigh_any), and every tile is looked at again
+    int up = -1;
+    __half2 least_d = __half2half2(__ushort_as_half(0)), most_d = __half2half2(__float2half_rn(-1.0f));
     int slot = 0, fill = T::kStages - 1;
     for (int i = 0; i < tiles; ++i) {
         copies_wait<T::kStages - 2>();
@@ -623,7 +702,12 @@ attend_kernel(const AttendArgs a) {
         float raw[T::kSub][2][NT], p[T::kSub][2][NT];
         T::scores(stage, s_q, rows, lane, raw);
         uint32_t d[Q8 ? T::kSub : 1][4][T::kPairs];
-        __half2 largest = __half2half2(__ushort_as_half(0));
+        __half2 largest = __half2half2(__ushort_as_half(0)), smallest = __half2half2(__ushort_as_half(0x3c00));
+        auto look = [&](const __half2 &scales) {
+            const __half2 size = __habs2(scales);
+            largest = __hmax2(largest, size);
+            smallest = __hmin2(smallest, __hadd2(size, __heq2(size, __half2half2(__ushort_as_half(0)))));
+        };
         if constexpr (Q8) {
 #pragma unroll
             for (int s = 0; s < T::kSub; ++s)
@@ -633,19 +717,17 @@ attend_kernel(const AttendArgs a) {
                     T::load_scales(stage + 2 * T::kPlane + T::kScales, at, NB % 2 ? s_rows[at] : 0u, d[s][j]);
                     if constexpr (NB % 2)
 #pragma unroll
-                        for (int c = 0; c < T::kPairs; ++c)
-                            largest = __hmax2(largest, __habs2(reinterpret_cast<const __half2 &>(d[s][j][c])));
+                        for (int c = 0; c < T::kPairs; ++c) look(reinterpret_cast<const __half2 &>(d[s][j][c]));
                 }
             if constexpr (NB % 2 == 0) {  // the words hold scales alone: a lane looks at a part of them
                 constexpr int kWords = T::kTokens * T::kScaleWords;  // 48 where d is 192; row numbers lie behind
                 const __half2 *words = reinterpret_cast<const __half2 *>(stage + 2 * T::kPlane + T::kScales);
 #pragma unroll
                 for (int c = 0; c < kWords; c += 32)
-                    if (kWords % 32 == 0 || c + lane < kWords)
-                        largest = __hmax2(largest, __habs2(words[c + lane]));
+                    if (kWords % 32 == 0 || c + lane < kWords) look(words[c + lane]);
             }
         }
-        bool move = Q8 && !__hble2(largest, most_d);
+        bool move = Q8 && !(__hble2(largest, most_d) && __hbge2(smallest, least_d));
 #pragma unroll
         for (int s = 0; s < T::kSub; ++s)
 #pragma unroll
@@ -657,19 +739,17 @@ attend_kernel(const AttendArgs a) {
                     move |= p[s][j][n] > 4.0f;
                 }
         if (__any_sync(0xffffffffu, move)) {
-            float ratio = 1.0f;  // of the new power of two that the outputs are held times to the old
             if constexpr (Q8) {
-                // weights up to 2^4 times lift times d 2^lift_d stay below
-                // 2^15: tiny scales are taken up, scales above 1 take lift down
-                uint32_t bits = reinterpret_cast<const uint32_t &>(largest);
-                bits = __reduce_max_sync(0xffffffffu, max(bits & 0xffffu, bits >> 16));
-                const int e = (int)(bits >> 10);  // the scale is below 2^(e - 14)
-                const float before = lift * exp2i(lift_d);
-                lift_d = e < 1 ? 14 : e < 8 ? 7 : 0;
-                lift = T::kLift * exp2i(-max(e - 14, 0));
-                ratio = lift * exp2i(lift_d) / before;
-                most_d = __half2half2(__ushort_as_half((unsigned short)(
-                    lift_d == 14 ? 0x03ff : lift_d == 7 ? 0x1fff : max(e << 10 | 0x3ff, 0x3c00))));
+                // The largest weight so far is 1 to 2^4: times kLift and a scale
+                // of 2^-14 to 1 it keeps 22 bits and stays below 2^15.
+                auto halves = [](const __half2 &x) { return reinterpret_cast<const uint32_t &>(x); };
+                const uint32_t most = __reduce_max_sync(0xffffffffu, max(halves(largest) & 0xffffu, halves(largest) >> 16));
+                const uint32_t least =
+                    __reduce_min_sync(0xffffffffu, min(halves(smallest) & 0xffffu, halves(smallest) >> 16));
+                // f16: 0x3c00 is 1, 0x1400 is 2^-10, 0x0400 is 2^-14, and none above 0 is below 2^-24
+                up = most <= 0x1400u ? 10 : most <= 0x3c00u && least >= 0x0400u ? 0 : -1;
+                most_d = up < 0 ? __half2half2(__float2half_rn(-1.0f)) : __half2half2(__ushort_as_half(up ? 0x1400 : 0x3c00));
+                least_d = __half2half2(__ushort_as_half(up ? 0 : 0x0400));
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -686,7 +766,7 @@ attend_kernel(const AttendArgs a) {
 #pragma unroll
                 for (int c = 0; c < T::kRowsOut; ++c)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) o[c][n][j] *= alpha * ratio;
+                    for (int j = 0; j < 2; ++j) o[c][n][j] *= alpha;
 #pragma unroll
                 for (int s = 0; s < T::kSub; ++s)
 #pragma unroll
@@ -703,8 +783,8 @@ attend_kernel(const AttendArgs a) {
                     if (!whole && rows[s][j] == kNoRow) p[s][j][n] = 0.0f;
                     l[n] += p[s][j][n];
                 }
-        if (Q8 && lift_d > 0) {
-            const __half2 f = __half2half2(__float2half_rn(exp2i(lift_d)));
+        if (Q8 && up > 0) {
+            const __half2 f = __half2half2(__float2half_rn(1024.0f));
 #pragma unroll
             for (int s = 0; s < (Q8 ? T::kSub : 1); ++s)
 #pragma unroll
@@ -715,9 +795,11 @@ attend_kernel(const AttendArgs a) {
                         d[s][j][c] = reinterpret_cast<const uint32_t &>(h);
                     }
         }
-        T::weigh(stage, lane, p, lift, d, o);
+        if (Q8 && up < 0)
+            T::weigh_any(stage, lane, p, d, o);
+        else
+            T::weigh(stage, lane, p, d, up, o);
     }
-    const float lift_inv = 1.0f / (lift * exp2i(lift_d));
 
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -733,7 +815,7 @@ attend_kernel(const AttendArgs a) {
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                s_o[(warp * H + 4 * n + t) * D + T::element(c, i, g)] = o[c][n][i] * lift_inv;
+                s_o[(warp * H + 4 * n + t) * D + T::element(c, i, g)] = o[c][n][i];
     __syncthreads();
     const bool wide = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)a.ldo * 4) & 15) == 0;
     auto finish = [&](int h, int e, float top, float sum, const float (&acc)[4]) {

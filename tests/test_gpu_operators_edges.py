@@ -78,6 +78,96 @@ def test_attention_of_long_sequences_without_splits(qmm, torch, fmt, d, kv_heads
     assert float((lse.double() - np.log(n)).abs().max()) <= (6 * tiles ** 0.5 / 3 + 16) * EPS32
 
 
+def check_elements(qmm, g, fmt, planes, heads, n, reach, q_scale):
+    """One sequence over the planes' pages in a row: every element of the output against its own weighted
+    mean of |v|, not the head's largest.  The weights' relative error as in attention_ref; and each
+    token's product of a weight and a scale (f16: its weight alone), held as two f16 numbers, keeps 2^-36
+    of `reach` in units of the largest weight (None: of the block's largest product), twice that where
+    both are rounded."""
+    kv_heads, ps, d = planes[0].shape[1:]
+    q = (q_scale * g.standard_normal((1, heads * d))).astype(np.float32)
+    table = np.arange(len(planes[0]), dtype=np.int32)[None]
+    out, lse = run_attention(qmm, fmt, up(q), [up(p) for p in planes], up(table), up(np.array([n], np.int32)))
+    out = out.cpu().numpy().astype(np.float64).reshape(heads, d)
+    pos = np.arange(n)
+    keys, values = base.cache_values(fmt, planes)
+    scale = np.float64(np.float32(d ** -0.5))
+    for h in range(heads):
+        kk, vv = (c[pos // ps, h // (heads // kv_heads), pos % ps] for c in (keys, values))
+        qh = q.reshape(heads, d)[h].astype(np.float64)
+        s = kk @ qh * scale
+        off = ((d / 8 + 16) * EPS32 * scale * (np.abs(kk) @ np.abs(qh)).max() +
+               scale * d * 2.0 ** -22 * np.abs(qh).max() * np.abs(kk).max() + 2.0 ** -20)
+        p = np.exp(s - s.max())
+        if fmt == "f16":
+            kept = reach * np.abs(vv).sum(0)
+        else:
+            where = pos // ps, h // (heads // kv_heads), pos % ps
+            codes, scales = planes[2][where].astype(np.float64), planes[3][where].astype(np.float64)
+            most = (p[:, None] * np.abs(scales)).max(0) if reach is None else np.full(d // 32, reach)
+            kept = np.repeat(most, 32) * np.abs(codes).sum(0)
+        tol = ((2 * off + 64 * EPS32) * (p @ np.abs(vv)) + 2.0 ** -35 * kept) / p.sum()
+        assert (np.abs(out[h] - p @ vv / p.sum()) <= tol).all()
+
+
+def scales_apart(g, kind, shape):
+    """Value scales, and `reach` of check_elements."""
+    u = 0.5 + g.random(shape)
+    if kind == "blocks":  # of one token: six and three powers of ten apart
+        return u * np.array([30, 3e-5, 0.03, 8e3])[np.arange(shape[-1]) % 4], None
+    if kind == "a block of zeros":
+        return u * (np.arange(shape[-1]) % 2) * 50, None
+    if kind == "anything":
+        return np.exp(g.uniform(np.log(1e-7), np.log(6e4), shape)), None
+    if kind == "stretches":  # along the sequence: tiny, ordinary, large, small
+        pages = np.arange(shape[0]) // 4 % 4
+        return u * np.array([1e-6, 0.02, 3e4, 3e-4])[pages].reshape(-1, 1, 1, 1), 1.0
+    if kind == "edges":
+        return np.array([2.0 ** -14, 2.0 ** -10, 1.0, 0.0])[g.integers(0, 4, shape)], 1.0
+    if kind == "subnormal":
+        return u * 3e-6, 2.0 ** -10
+    if kind == "one large token":
+        s = u * 1e-3
+        s[1, :, 3] = 3e4
+        return s, 1.0
+    raise ValueError(kind)
+
+
+@pytest.mark.parametrize("kind", ["blocks", "a block of zeros", "anything", "stretches", "edges", "subnormal",
+                                  "one large token"])
+@pytest.mark.parametrize("heads,d", [(4, 128), (8, 64), (3, 96), (6, 192), (5, 256)])
+@pytest.mark.parametrize("q_scale", [0.0, 1.0])
+def test_attention_q8_0_value_scales_far_apart(qmm, kind, heads, d, q_scale):
+    g = rng_of(33, d, heads)
+    planes = make_cache(g, "q8_0", 40, 1, 16, d)
+    scales, reach = scales_apart(g, kind, planes[3].shape)
+    planes[3] = scales.astype(np.float16)
+    check_elements(qmm, g, "q8_0", planes, heads, 635, reach, q_scale)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_q8_0_of_a_large_scale_without_weight(qmm, sign):
+    """A token whose score is far below the others' and whose scale is 3e7 times theirs: nothing of it
+    may be seen, and the others keep their digits."""
+    g = rng_of(34)
+    planes = make_cache(g, "q8_0", 19, 1, 16, 64)
+    planes[3][:] = np.float16(1e-3)
+    planes[3][5, 0, 9] = np.float16(3e4)
+    planes[0][5, 0, 9], planes[1][5, 0, 9] = -127 * sign, np.float16(0.3)
+    q = np.full((1, 4 * 64), sign, np.float32)
+    check_attention(qmm, 34, "q8_0", 4, 1, 64, 16, [300], q=q, planes=planes,
+                    table=np.arange(19, dtype=np.int32)[None])
+
+
+@pytest.mark.parametrize("heads,d", [(4, 128), (8, 64), (3, 96), (5, 256)])
+@pytest.mark.parametrize("q_scale", [0.0, 1.0])
+def test_attention_f16_values_far_apart(qmm, heads, d, q_scale):
+    g = rng_of(35, d, heads)
+    planes = make_cache(g, "f16", 40, 1, 16, d)
+    planes[1] = (planes[1] * np.exp(g.uniform(np.log(1e-4), np.log(1e4), d))).astype(np.float16)
+    check_elements(qmm, g, "f16", planes, heads, 635, 1.0, q_scale)
+
+
 @pytest.mark.parametrize("d", [160, 192, 224])
 def test_attention_q8_0_in_pages_of_large_row_numbers(qmm, d):
     g = rng_of(32, d)
