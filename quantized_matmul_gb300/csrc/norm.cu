@@ -12,6 +12,8 @@
 // rounding are IEEE (the codes' rounding to 8 bits is the format's).
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "qmm_internal.h"
 
 namespace qmm {
@@ -199,10 +201,11 @@ rms_norm_kernel(const NormArgs a, bool pdl) {
 #pragma unroll
             for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float d = __fdiv_rn(m, 127.0f);
-            // The quotients by d's reciprocal are off by at most 2^-16 (three
-            // roundings of a number up to 127), so they round as the IEEE
-            // quotients do unless one is that near to a half; only then, and
-            // for a d whose reciprocal leaves f32's normal range, divide.
+            // The quotients by d's reciprocal differ from the IEEE ones by less
+            // than 2^-15 (three roundings of a number up to 127), so they round
+            // as those do unless one is that near to a half; only then (within
+            // 2^-14), and for a d whose reciprocal leaves f32's normal range,
+            // divide.
             uint32_t q = 0;
             float off = 1.0f;
             if (d >= 1e-37f) {
@@ -232,14 +235,18 @@ rms_norm_kernel(const NormArgs a, bool pdl) {
         int sum = 0;
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            // scale * 0 is 0: a row of zeros needs no case of its own
+            // a row of zeros has scale 0 and needs no case of its own
             const float4 t = make_float4(__fmul_rn(h[e].x, scale), __fmul_rn(h[e].y, scale),
                                          __fmul_rn(h[e].z, scale), __fmul_rn(h[e].w, scale));
             float off;
             uint32_t q = codes4(t, off);
-            if (off >= 0.5f) q = codes4_exact(t);
-            if (at(e) < k) codes[at(e) / 4] = q;
-            sum = __dp4a((int)q, 0x01010101, sum);
+            // 127 / amax overflows below 3.7e-37: the products are infinite
+            // (NaN where y is 0), which only the exact codes clamp
+            if (off >= 0.5f || scale > FLT_MAX) q = codes4_exact(t);
+            if (at(e) < k) {
+                codes[at(e) / 4] = q;
+                sum = __dp4a((int)q, 0x01010101, sum);
+            }
         }
         sum = __reduce_add_sync(0xffffffffu, sum);
         if (lane == 0) s_sum[warp] = sum;

@@ -16,6 +16,47 @@ def torch():
 
 
 # ---------------------------------------------------------------------------
+# norm
+
+def exact_norm(g, m, k, least, most):
+    """x of +-1 and +-7 with a mean square of 16, in rows; a weight from 2^least to 2^most; and y = x / 4
+    * w, which with eps = 0 has no rounding but the last product's, in whatever order the squares add up."""
+    x = np.where(np.arange(k) < 5 * k // 16, 7, 1) * g.choice([-1, 1], (m, k))
+    x = g.permuted(x, axis=1).astype(np.float32)
+    w = (np.exp2(g.uniform(least, most, k)) * g.choice([-1, 1], k)).astype(np.float32)
+    return x, w, (x / np.float32(4)) * w
+
+
+@pytest.mark.parametrize("k", [32, 64, 256, 1024, 4096, 8192, 11008, 16384, 16416, 32768])
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("least,most", [(-3, 3), (-30, 0), (-141, -130), (90, 110)])
+def test_rms_norm_gives_the_quantizers_codes(qmm, torch, k, aligned, least, most):
+    """y is known to the bit, so codes, scales and sums are those of the quantizers on y, also where the
+    scales are subnormal or a BitNet scale overflows."""
+    m = 3
+    x, w, y = exact_norm(rng_of(40, k, 200 + least), m, k, least, most)
+    xs = up(x) if aligned else base.strided(x, 1, k + 3)
+    assert torch.equal(xs, up(x))
+    aq, ad, _ = qmm.rms_norm_q8_0(xs, up(w), 0.0)
+    want = qmm.quantize_act_q8_0(up(y))
+    assert torch.equal(aq, want[0]) and torch.equal(ad.view(torch.int16), want[1].view(torch.int16))
+    got = qmm.rms_norm_bitnet(xs, up(w), 0.0)
+    want = qmm.quantize_act_bitnet(up(y))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("k", [64, 2560, 4096, 11008, 20000])
+@pytest.mark.parametrize("aligned", [True, False])
+def test_rms_norm_of_rows_next_to_zero_and_zeros(qmm, torch, k, aligned):
+    """Half of the weights are 0, so infinite BitNet scales meet zeros: the quantizer's codes again."""
+    x, w, y = exact_norm(rng_of(41, k), 2, k, -140, -138)
+    w[::2], y[:, ::2] = 0, 0
+    xs = up(x) if aligned else base.strided(x, 1, k + 3)
+    for got, want in zip(qmm.rms_norm_bitnet(xs, up(w), 0.0), qmm.quantize_act_bitnet(up(y))):
+        assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------------------
 # attention
 
 @pytest.mark.parametrize("fmt", ["f16", "q8_0"])
