@@ -16,6 +16,9 @@ Tensor conventions (row-major, contiguous, on the current CUDA device):
 Around the products, for a decode step: the norm with the residual's addition
 and an 8-bit output (rms_norm_q8_0, rms_norm_bitnet), the paged key-value cache
 (kv_append_*, paged_attention_*) and the logits' log probabilities (log_probs).
+Outputs that such a call makes itself share one allocation where they take
+256 KB or less together: keeping or saving one of them keeps or saves all
+(clone() what is to outlive the rest).
 """
 from __future__ import annotations
 
@@ -666,7 +669,8 @@ def rms_norm_q8_0(x, weight, eps: float = 1e-5, residual=None, h=None, aq=None, 
     """Root-mean-square norm with the residual's addition and Q8_0 output, one
     launch: h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight, and y's
     codes.  Returns (aq int8 [m, k], ad fp16 [m, k/32], h f32 [m, k]), ready
-    for the Q4_0 and Q8_0 products.
+    for the Q4_0 and Q8_0 products (small outputs share an allocation, see the
+    module's notes).
 
     h: where to write the sum (may be x or residual itself, for a residual
     stream updated in place); without a residual and without h, h is x.  x,
@@ -723,7 +727,8 @@ def paged_attention_f16(q, kc, vc, table, lens, max_len=None, scale=None, window
     of lens known on the host (default: the table's capacity); the work is
     split over it.  window: attend to the last `window` tokens only (0: all).
     scale: default d ** -0.5.  Returns (out float32 [batch, heads * d], lse
-    float32 [batch, heads]); a sequence of length 0 gives 0 and -inf."""
+    float32 [batch, heads], small ones in one allocation); a sequence of length 0
+    gives 0 and -inf."""
     return (_fast or _binding()).paged_attention_f16(q, kc, vc, table, lens, max_len, scale, window, out,
                                                      lse, workspace)
 
@@ -747,8 +752,9 @@ def log_probs(logits, tokens=None, top_k: int = 0):
 
     tokens: int32 [m, t] (or [m]) word numbers, or None.  Returns
     (token_logprobs f32 like tokens or None, entropy f32 [m], top_ids int32
-    [m, top_k], top_logprobs f32 [m, top_k]); alternatives in falling order,
-    the lower number first among equal logits, top_k <= 32."""
+    [m, top_k], top_logprobs f32 [m, top_k]), small ones in one allocation;
+    alternatives in falling order, the lower number first among equal logits,
+    top_k <= 32."""
     return (_fast or _binding()).log_probs(logits, tokens, top_k)
 
 

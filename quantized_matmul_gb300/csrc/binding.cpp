@@ -116,13 +116,19 @@ at::Tensor out(PyObject *o, at::IntArrayRef shape, at::ScalarType type, const at
 }
 
 // Outputs of one call that share an allocation, each on 64 bytes: an
-// allocation costs about 0.4 us of a call's 5 to 7.
+// allocation costs about 0.4 us of a call's 5 to 7.  Who keeps one of them
+// keeps all, so calls with more bytes than kMost give each its own.
 struct Shared {
-    at::Tensor buffer;
+    static constexpr int64_t kMost = 1 << 18;
+    at::TensorOptions options;
+    at::Tensor buffer;  // undefined: each its own
     int64_t used = 0;
     static int64_t bytes(int64_t count, int64_t size) { return (count * size + 63) & ~(int64_t)63; }
-    Shared(const at::Tensor &like, int64_t bytes) : buffer(at::empty({bytes}, like.options().dtype(at::kByte))) {}
+    Shared(const at::Tensor &like, int64_t bytes) : options(like.options()) {
+        if (bytes <= kMost) buffer = at::empty({bytes}, options.dtype(at::kByte));
+    }
     at::Tensor take(at::IntArrayRef shape, at::ScalarType type) {
+        if (!buffer.defined()) return at::empty(shape, options.dtype(type));
         at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
             c10::Storage(buffer.storage()), buffer.key_set(), c10::scalarTypeToTypeMeta(type));
         t.unsafeGetTensorImpl()->set_storage_offset(used / (int64_t)c10::elementSize(type));
@@ -184,11 +190,10 @@ Norm norm_args(PyObject *const *a, int outputs, int64_t per_block, int64_t per_r
     if (a[3] != Py_None) n.rr = rows(a[3], n.m, n.k, "residual");
     bool made = true;
     for (int i = 0; i < outputs; ++i) made &= a[5 + i] == Py_None;
-    // a large sum, which outlives the codes, has memory of its own
-    const int64_t sum_bytes = Shared::bytes(n.m * n.k, 4);
-    const bool with_sum = made && a[4] == Py_None && n.rr.p && sum_bytes <= (1 << 20);
+    const bool with_sum = made && a[4] == Py_None && n.rr.p;
     if (made)
-        n.shared.emplace(n.x, (with_sum ? sum_bytes : 0) + n.m * (n.k + n.k / 32 * per_block + per_row) + 64 * outputs);
+        n.shared.emplace(n.x, (with_sum ? Shared::bytes(n.m * n.k, 4) : 0) +
+                                  n.m * (n.k + n.k / 32 * per_block + per_row) + 64 * outputs);
     if (a[4] != Py_None) {
         n.h = tensor(a[4], at::kFloat, "h");
         n.hr = rows(n.h, n.m, n.k, "h");

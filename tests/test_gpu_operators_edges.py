@@ -249,3 +249,33 @@ def test_log_probs_join_of_many_alternatives(qmm, torch, m, n, low):
     for _ in range(200):
         got = qmm.log_probs(view, top_k=32)
         assert all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+
+
+# ---------------------------------------------------------------------------
+# outputs
+
+def test_large_outputs_have_memory_of_their_own(qmm, torch):
+    """Keeping one output of a large call keeps only that one's bytes; small calls' outputs share 256 KB at
+    most.  Contents are right in either form."""
+    def owned(t):
+        return t.untyped_storage().nbytes()
+
+    def z(*shape, dtype=torch.float32):
+        return torch.zeros(shape, dtype=dtype, device="cuda")
+
+    for m in (1, 16, 64, 2048):
+        x, w = torch.ones((m, 4096), device="cuda"), torch.ones(4096, device="cuda")
+        calls = [qmm.rms_norm_q8_0(x, w, residual=x), qmm.rms_norm_bitnet(x, w, residual=x),
+                 qmm.rms_norm_bitnet(x, w)[:3],
+                 qmm.log_probs(x, z(m, 8, dtype=torch.int32), top_k=32)]
+        cache, table = z(4, 2, 16, 128, dtype=torch.float16), z(m, 1, dtype=torch.int32)
+        calls.append(qmm.paged_attention_f16(z(m, 16 * 128), cache, cache, table, z(m, dtype=torch.int32) + 5))
+        for outputs in calls:
+            size = sum(t.numel() * t.element_size() for t in outputs)
+            for t in outputs:
+                assert owned(t) <= max(t.numel() * t.element_size(), min(1 << 18, size + 64 * len(outputs)))
+            if size > 1 << 18:
+                assert len({t.untyped_storage().data_ptr() for t in outputs}) == len(outputs)
+        assert torch.equal(calls[0][2], x + x) and (calls[0][0] == 127).all()
+        assert torch.equal(calls[1][2], calls[1][0].int().sum(-1, dtype=torch.int32))
+        assert (calls[3][2] == torch.arange(32, device="cuda")).all() and (calls[4][0] == 0).all()
