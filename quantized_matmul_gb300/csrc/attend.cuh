@@ -993,6 +993,7 @@ cudaError_t launch_attend_nb(const AttendArgs &a, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = a.cluster ? 2 : 1;
+    if (a.cluster) g_exchange_used.store(true, std::memory_order_relaxed);
     e = cudaLaunchKernelEx(&cfg, attend_kernel<NB, Q8, NT>, a);
     if (e != cudaSuccess || a.splits == 1 || a.cluster) return e;
     const dim3 join((unsigned)a.heads, (unsigned)a.batch);

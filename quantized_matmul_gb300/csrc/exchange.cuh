@@ -12,12 +12,17 @@
 // and, after waiting as long again for what is on its way, gives up.
 #pragma once
 
+#include <atomic>
+
 #include "qmm_internal.h"
 
 namespace qmm {
 namespace {
 
 __device__ unsigned int g_exchange_error = 0;  // of this translation unit's kernels
+// Whether any of them was launched (or captured) with an exchange: else their
+// error word is not read, which takes about 10 us of qmm_check_device_error.
+std::atomic<bool> g_exchange_used{false};
 
 __device__ __forceinline__ uint32_t shared_addr(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -100,6 +105,8 @@ __device__ __forceinline__ bool exchange_wait(uint64_t *bar, uint32_t limit) {
 
 cudaError_t exchange_read_and_clear_error(unsigned int *word, cudaStream_t s) {
     const unsigned int zero = 0;
+    *word = 0;
+    if (!g_exchange_used.load(std::memory_order_relaxed)) return cudaSuccess;
     cudaError_t e = cudaMemcpyFromSymbolAsync(word, g_exchange_error, sizeof zero, 0, cudaMemcpyDeviceToHost, s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess || !*word) return e;

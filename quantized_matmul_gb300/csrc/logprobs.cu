@@ -574,6 +574,7 @@ cudaError_t launch(const LogProbsArgs &a, int ranks, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = ranks > 1 ? 2 : 1;
+    if (ranks > 1) g_exchange_used.store(true, std::memory_order_relaxed);
     return cudaLaunchKernelEx(&cfg, log_probs_kernel<kStages, VEC>, a, slice);
 }
 

@@ -279,3 +279,45 @@ def test_large_outputs_have_memory_of_their_own(qmm, torch):
         assert torch.equal(calls[0][2], x + x) and (calls[0][0] == 127).all()
         assert torch.equal(calls[1][2], calls[1][0].int().sum(-1, dtype=torch.int32))
         assert (calls[3][2] == torch.arange(32, device="cuda")).all() and (calls[4][0] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# errors
+
+CHECK_TWICE = """
+import time
+import torch
+import quantized_matmul_gb300 as q
+
+def check():
+    times = []
+    for _ in range(300):
+        t = time.perf_counter()
+        assert q.check_device_error() == 0
+        times.append(time.perf_counter() - t)
+    return sorted(times)[len(times) // 2]
+
+torch.zeros(1, device="cuda")
+check()
+before = check()
+lens, table = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([500], [list(range(32))]))
+f16 = torch.ones(32, 1, 16, 128, dtype=torch.float16, device="cuda")
+codes, scales = f16.to(torch.int8), torch.ones(32, 1, 16, 4, dtype=torch.float16, device="cuda")
+x = torch.ones(1, 128, device="cuda")
+q.paged_attention_f16(x, f16, f16, table, lens)
+q.paged_attention_q8_0(x, codes, scales, codes, scales, table, lens)
+q.log_probs(torch.zeros(1, 20000, device="cuda"))
+print(before / check())
+"""
+
+
+def test_the_error_check_reads_no_words_of_kernels_that_never_ran():
+    """Five words before the first exchange within a cluster, eight after: a process that only runs the
+    products pays for those (read apart, each takes about as long)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CHECK_TWICE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    assert float(r.stdout) < 0.85, r.stdout
