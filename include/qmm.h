@@ -484,8 +484,12 @@ qmm_status qmm_kv_append_q8_0(const float *k, int64_t ldk, const float *v, int64
  *   bytes, 16-byte aligned (NULL allowed when that size is 0), for the splits'
  *   partial results.  Not reentrant on one workspace.
  *   q and what is attended to must be finite.
- * Everything is f32 precision: q and the softmax weights enter the tensor
- * cores as two f16 parts each, the cache's values exactly. */
+ * Scores, softmax statistics and sums are f32.  The cache's values enter the
+ * tensor cores exactly; q, the softmax weights and (Q8_0) the weights' products
+ * with the values' scales as two f16 parts, which keep 22 bits, or 2^-36 of the
+ * largest weight (times the block's largest scale, where that is above 1).  An
+ * exponential is good to 2 units in the last place.  Results do not depend on
+ * where the pages lie. */
 size_t qmm_paged_attention_workspace_bytes(int64_t batch, int64_t heads, int64_t kv_heads,
                                            int64_t d, int64_t max_len);
 qmm_status qmm_paged_attention_f16(const float *q, int64_t ldq, const uint16_t *kc,

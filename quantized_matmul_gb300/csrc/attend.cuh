@@ -13,21 +13,25 @@
 // token that is not attended to reads nothing and fills in zeros, so what the
 // cache holds there never enters the arithmetic.
 //
-// Measured (32 query and 8 key heads of 128): 131067 tokens f16 in 87 us (6.2
+// Measured (32 query and 8 key heads of 128): 131067 tokens f16 in 88 us (6.1
 // TB/s; the copies alone take as long), 64 ragged sequences of up to 4096
-// tokens Q8_0 in 62 us (4.7 TB/s; the copies alone take 54, the rest is the
-// instructions that turn codes into f16), 577 tokens f16 in 4.3 us.  Copying
-// each row in bulk, one instruction a row counted by an mbarrier, in place of
-// 16 bytes a lane took 101 us, and 6.1 for the 577.
+// tokens Q8_0 in 63 us (4.7 TB/s; the copies alone take 54; issue is at 61% and
+// DRAM at 60%: half of the CTAs are empty, and 16 warps a SM hide neither the
+// loads nor the chain from codes to f16 to products), 577 tokens f16 in 4.2 us.
+// Copying each row in bulk, one instruction a row counted by an mbarrier, in
+// place of 16 bytes a lane took 101 us, and 6.1 for the 577.
 //
 // Precision: q and the softmax weights are f32, the cache's values are exact
 // in f16 (int8 codes too).  Each f32 factor enters the MMA as two f16 numbers
-// hi + lo, hi = f16(f), lo = f16(f - hi), which keep 22 bits.  The cache is
-// the MMA's A operand (16 tokens for the scores, 16 elements of the values
-// for the output); the 8 columns of B are 4 heads' hi and lo in turn, so a
-// lane's two neighbouring accumulators add up to a head's product.  The MMA
-// sums one tile's tokens, f32 additions the tiles.  Powers of two keep both in
-// f16's range: a head's q is scaled to its largest element, the weights by 2^11.
+// hi + lo, hi = f16(f), lo = f16(f - hi), which keep 22 bits (of a weight at
+// least 2^-36 of the largest); a third part would take columns of B from other
+// heads, and the outputs' errors are 3e-7 to 9e-7 of 64 bits as it is, a plain
+// f32 form's 4e-7 to 1.8e-6.  The cache is the MMA's A operand (16 tokens for
+// the scores, 16 elements of the values for the output); the 8 columns of B are
+// 4 heads' hi and lo in turn, so a lane's two neighbouring accumulators add up
+// to a head's product.  The MMA sums one tile's tokens, f32 additions the tiles.
+// Powers of two keep both in f16's range: a head's q is scaled to its largest
+// element, the weights by 2^11.
 //
 // The softmax's base need not be the running maximum: weights up to 2^4 fit,
 // so the base (and with it the outputs so far) moves only when a score passes

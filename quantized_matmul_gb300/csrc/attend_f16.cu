@@ -10,7 +10,7 @@ namespace {
 constexpr int64_t kSpanUnit = 128;
 // Up to this many tokens a cluster of 8 CTAs a head finishes before as many
 // splits as there is room for and their join do (32 query and 8 key heads of
-// 128, f16, 577 tokens: 4.3 us; 1024 tokens: 4.3 against 7 us).  A cluster's
+// 128, f16, 577 tokens: 4.2 us; 1024 tokens: 4.3 against 7 us).  A cluster's
 // CTAs need their SMs at once, so large batches are split.
 constexpr int64_t kShort = 1024;
 

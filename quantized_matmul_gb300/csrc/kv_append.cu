@@ -6,9 +6,11 @@
 // elements each, so eight threads hold a block and its maximum takes three
 // shuffles; a thread has its key's and its value's loads in flight together.
 // Bound by the bytes (8 read, 4 or 2.125 written an element pair) for many
-// tokens (2048 tokens of 8 heads of 128, f16: 3.7 us, 6.6 TB/s) and by the
-// launch for a few (16 tokens, Q8_0: 2.0 us).  With the key and the value one
-// after the other and divisions it took 8.0 us for the 2048.
+// tokens (2048 tokens of 8 heads of 128, f16: 3.8 us with rows that L2 still
+// holds, as behind the projection that wrote them; 5.9 us, 4.3 TB/s, from HBM;
+// Q8_0 7.6 us from HBM) and by the launch for a few (16 tokens, Q8_0: 2.0 us).
+// With the key and the value one after the other and divisions it took 8.0 us
+// for the 2048 of L2.
 #include "kvcache.cuh"
 
 namespace qmm {

@@ -20,7 +20,7 @@
 // alternatives: 47 us, 5.6 TB/s): all 512 CTAs are resident at once, three or
 // four a SM, and reach their tails together.  Two, four and eight CTAs a row
 // would spread them evenly, but their tails cost more than that gives (1.04,
-// 1.1 and 1.4 times as long).  Few rows are bound by latency: one row takes 6.5
+// 1.1 and 1.4 times as long).  Few rows are bound by latency: one row takes 6.4
 // us with 20 alternatives, most of it the chain of barriers, shuffles and the
 // cluster's exchange behind a read of 1.3 us.  Code that runs once counts
 // there, so loops that are rarely taken stay rolled.
